@@ -70,6 +70,13 @@ __device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// What k_few_prep writes (x_few, x_sums, row_x).  It may still be running when
+// this kernel starts, so its results are read after grid_wait() and by
+// ordinary loads: the read-only path (__ldg) is for data that nothing writes
+// while a kernel runs, and the compiler may move such loads over the wait.
+template <typename T>
+__device__ __forceinline__ T few_prepared(const T* p) { return *p; }
+
 // What a lane loads of one weight row for one slice.
 template <int FMT>
 struct FewRaw {
@@ -295,15 +302,15 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
         auto load_sums = [&](int b, int it) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float* q = sp[b][c] + it * NS;
+                const float* sums = sp[b][c] + it * NS;
                 if constexpr (NS == 1) {
-                    xs[b][c][0] = __ldg(q);
+                    xs[b][c][0] = few_prepared(sums);
                 } else if constexpr (NS == 2) {
-                    const float2 v = __ldg(reinterpret_cast<const float2*>(q));
+                    const float2 v = few_prepared(reinterpret_cast<const float2*>(sums));
                     xs[b][c][0] = v.x;
                     xs[b][c][1] = v.y;
                 } else {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(q));
+                    const float4 v = few_prepared(reinterpret_cast<const float4*>(sums));
                     xs[b][c][0] = v.x;
                     xs[b][c][1] = v.y;
                     xs[b][c][2] = v.z;
@@ -316,7 +323,7 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
             xp[b] = reinterpret_cast<const uint4*>(a.x_few) +
                     static_cast<int64_t>(t.row0 + min(8 * b + gid, t.n - 1)) * NI * 16 + tig;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) x[h][b] = __ldg(xp[b] + kw * 16 + 4 * h);
+            for (int h = 0; h < 4; ++h) x[h][b] = few_prepared(xp[b] + kw * 16 + 4 * h);
             if (INT) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -347,7 +354,7 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                     for (int b = 0; b < NB; ++b) {
                         few_mma(d[b], p0[0], p1[0], p0[1], p1[1], x[h][b].x, x[h][b].y);
                         few_mma(d[b], p0[2], p1[2], p0[3], p1[3], x[h][b].z, x[h][b].w);
-                        if (tl == 1) x[h][b] = __ldg(xp[b] + ahead * 16 + 4 * h);
+                        if (tl == 1) x[h][b] = few_prepared(xp[b] + ahead * 16 + 4 * h);
                     }
                     if (!INT && h == 3) {
 #pragma unroll
@@ -407,7 +414,7 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                 const int tok = v >> 4, r = v & 15;
                 const int64_t f = static_cast<int64_t>(t.m) * 16 + r;
                 if (tok < t.n && f < a.O) {
-                    const float sx = __ldg(a.row_x + t.row0 + tok) * UNIT;
+                    const float sx = few_prepared(a.row_x + t.row0 + tok) * UNIT;
                     float g = sum(0, tok, r) * sx, u = sum(1, tok, r) * sx;
                     if (FMT == TQ_NVFP4_G16) {
                         g *= __ldg(a.gs[0] + t.e);
@@ -432,7 +439,7 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                 const int tok = v >> 5, r = v & 31;
                 const int64_t o = a.o_begin + static_cast<int64_t>(t.m) * 32 + r;
                 const bool live = tok < t.n && o < a.o_end;
-                float z = live ? sum(r >> 4, tok, r & 15) * (__ldg(a.row_x + t.row0 + tok) * UNIT) : 0.f;
+                float z = live ? sum(r >> 4, tok, r & 15) * (few_prepared(a.row_x + t.row0 + tok) * UNIT) : 0.f;
                 if (FMT == TQ_NVFP4_G16) z *= __ldg(a.gs[0] + t.e);
                 if (a.mode == ROWS_STORE) {
                     if (live) rows_put(a.y, (t.row0 + tok) * a.ldy + o, a.y_bf16, z);
