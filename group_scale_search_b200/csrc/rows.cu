@@ -8,7 +8,7 @@
 
 namespace tq {
 
-// ------------------------------------------------------------------ before: row factors and scale maxima
+// ------------------------------------------------------------------ before: row factors and the matrices' largest values
 
 constexpr int PREP_THREADS = 256;
 
@@ -48,6 +48,7 @@ struct PrepArgs {
     float* row_f;                  // gated backward: |dh|max |src|2
     // the blocks after them: parts of the matrices' scales
     const void* scales[2];
+    const uint8_t* zeros[2];       // int4, else null
     int64_t per_mat;               // scales of a matrix
     int E, e4m3;
     float* wmax;                   // [projections][E][rows_wmax_parts(E)]
@@ -116,15 +117,54 @@ __global__ void __launch_bounds__(PREP_THREADS) k_rows_prep(const __grid_constan
             if (q1 + threadIdx.x < p1) c = max(c, __ldg(q1 + threadIdx.x) & 0x7fu);
             m = e4m3_value(c);
         } else {
+            // |s| times the furthest a code may be from the zero-point (int4:
+            // 0 .. 15, and a zero-point is any byte; int3: -4 .. 3).  Four at a
+            // time between the ends: with one a load 1999 rows over 16 int3
+            // experts took 329 us, so 314.
             const float* s = static_cast<const float*>(a.scales[proj]) + e * a.per_mat;
-            // (an infinite or NaN scale is its own groups' matter)
-            for (int64_t i = lo + threadIdx.x; i < hi; i += 4 * PREP_THREADS) {
+            const uint8_t* z = a.zeros[proj] ? a.zeros[proj] + e * a.per_mat : nullptr;
+            const float *p0 = s + lo, *p1 = s + hi;
+            const float* q0 = reinterpret_cast<const float*>((reinterpret_cast<uintptr_t>(p0) + 15) & ~uintptr_t(15));
+            const float* q1 = reinterpret_cast<const float*>(reinterpret_cast<uintptr_t>(p1) & ~uintptr_t(15));
+            auto far4 = [&](uint32_t zz) { return z ? __vmaxu4(zz, __vsubus4(0x0f0f0f0fu, zz)) : 0x04040404u; };
+            auto take = [&](float v, uint32_t far) {   // (an infinite or NaN scale is its own groups' matter)
+                constexpr float MOST = 3.4028234e38f;
+                v = fabsf(v);
+                m = v <= MOST ? fmaxf(m, fminf(v * static_cast<float>(far & 0xffu), MOST)) : m;
+            };
+            if (q0 < q1) {
+                const float4* w = reinterpret_cast<const float4*>(q0);
+                const uint8_t* zw = z ? z + (q0 - s) : nullptr;
+                const bool words = (reinterpret_cast<uintptr_t>(zw) & 3) == 0;
+                const int64_t n = (q1 - q0) / 4;
+                for (int64_t i = threadIdx.x; i < n; i += 4 * PREP_THREADS) {
+                    float4 v[4];
+                    uint32_t zz[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float v = fabsf(__ldg(s + min(i + k * PREP_THREADS, hi - 1)));
-                    m = v <= 3.4028234e38f ? fmaxf(m, v) : m;
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t j = min(i + k * PREP_THREADS, n - 1);
+                        v[k] = __ldg(w + j);
+                        if (!z) zz[k] = 0u;
+                        else if (words) zz[k] = __ldg(reinterpret_cast<const uint32_t*>(zw) + j);
+                        else
+                            zz[k] = __ldg(zw + 4 * j) | (__ldg(zw + 4 * j + 1) << 8) | (__ldg(zw + 4 * j + 2) << 16) |
+                                    (static_cast<uint32_t>(__ldg(zw + 4 * j + 3)) << 24);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t far = far4(zz[k]);
+                        take(v[k].x, far);
+                        take(v[k].y, far >> 8);
+                        take(v[k].z, far >> 16);
+                        take(v[k].w, far >> 24);
+                    }
                 }
+            } else {
+                q0 = q1 = p1;
             }
+            auto one = [&](const float* p) { take(__ldg(p), far4(z ? __ldg(z + (p - s)) : 0u)); };
+            if (p0 + threadIdx.x < q0) one(p0 + threadIdx.x);   // (at most 3, or 7 in all)
+            if (q1 + threadIdx.x < p1) one(q1 + threadIdx.x);
         }
         m = block_max(m);
         if (threadIdx.x == 0) a.wmax[b] = m;
@@ -616,8 +656,8 @@ static tq_status few(int32_t fmt, RowsArgs& a, const tq_mat* X, const FewSpace& 
 }
 
 // What a forward launch needs beside the records: the tokens in f16 with their
-// powers of two, and the scales' maxima (integer formats, scaled kind; the
-// gated backward pass).
+// powers of two, and the matrices' largest values (integer formats, scaled
+// kind; the gated backward pass).
 struct ForwardSpace {
     uint16_t* x16;
     float* row_x;
@@ -687,6 +727,8 @@ static tq_status join(const RowsArgs& a, void* dx, int64_t ldx, cudaStream_t st)
 static tq_status prep(PrepArgs& p, const RowsArgs& a, int32_t fmt, cudaStream_t st) {
     p.scales[0] = a.scales[0];
     p.scales[1] = a.scales[1];
+    p.zeros[0] = a.zeros[0];
+    p.zeros[1] = a.zeros[1];
     p.per_mat = a.O * a.G;
     p.E = a.E;
     p.e4m3 = fmt == TQ_NVFP4_G16;

@@ -19,7 +19,7 @@ enum RowsMode {
 };
 
 constexpr float ROWS_PROB_SCALE = 1024.f;   // of ROWS_PROB's D
-// Partial maxima of a matrix's scales: enough blocks for one matrix, few of each
+// Partial maxima of a matrix's values: enough blocks for one matrix, few of each
 // where there are many.
 __host__ __device__ __forceinline__ int rows_wmax_parts(int E) { return E <= 2 ? 64 : E >= 32 ? 4 : 128 / E; }
 constexpr int ROWS_MAX_MATS = 1024;
@@ -51,7 +51,7 @@ struct RowsArgs {
     int64_t ldd;
     const float* row_f;             // [R]: gated backward |dh|max |x|2; matmul backward 2^c; loss backward dloss
     const float* row_x;             // [R]: forward: the power of two beside a token's f16 values
-    const float* wmax;              // [projections][E][rows_wmax_parts(E)]
+    const float* wmax;              // [projections][E][rows_wmax_parts(E)]: parts of a matrix's largest value (rows_wmax)
     const int64_t* labels;
     const float* lse;
     const uint16_t* x_few;          // few tokens: f16 in the kernel's order, [R][slices of 128 columns][256 bytes]
@@ -160,11 +160,6 @@ __host__ __device__ __forceinline__ Pow2 pow2_of(float x) {
     return r;
 }
 
-// Largest magnitude of a code's value (before the group scale).
-__host__ __device__ constexpr float code_max(int fmt) {
-    return is_int4(fmt) ? 15.f : fmt == TQ_INT3_G64_SYM ? 4.f : 6.f;
-}
-
 // The gated backward pass stores D as f16 (dg or du) * inv * 2^14 with inv the
 // inverse power of two of a bound on |dg| and |du|: |dh| <= dmax, |u|, |g| <=
 // |x|2 |What row|2 <= |x|2 sqrt(I) wm, |act'| <= 1.13, |act(g)| <= |g|.
@@ -256,7 +251,9 @@ __device__ __forceinline__ void rows_put(void* y, int64_t at, int bf16, float v)
     else static_cast<float*>(y)[at] = v;
 }
 
-// The largest scale magnitude of matrix e (both projections): a warp's work.
+// What bounds the values of matrix e (of both projections): the largest |s|
+// max(z, 15 - z) of int4 groups, whose zero-points are any byte, 4 |s| of int3
+// ones; NVFP4: the largest block scale.  A warp's work.
 __device__ __forceinline__ float rows_wmax(const RowsArgs& a, int e, int lane) {
     if (a.wmax == nullptr) return 1.f;
     float v = 0.f;
@@ -273,8 +270,9 @@ __device__ __forceinline__ float rows_wmax(const RowsArgs& a, int e, int lane) {
 // so both scales' product stands in it).
 template <int FMT>
 __device__ __forceinline__ float rows_bound_wm(const RowsArgs& a, int e, float wm) {
-    float b = wm * code_max(FMT);
-    if (FMT == TQ_NVFP4_G16 && a.projections == 2) b *= fabsf(__ldg(a.gs[0] + e)) * fabsf(__ldg(a.gs[1] + e));
+    if (FMT != TQ_NVFP4_G16) return wm;
+    float b = wm * 6.f;   // (E2M1's largest)
+    if (a.projections == 2) b *= fabsf(__ldg(a.gs[0] + e)) * fabsf(__ldg(a.gs[1] + e));
     return b;
 }
 

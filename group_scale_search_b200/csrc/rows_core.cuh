@@ -52,9 +52,9 @@
 //          at most 6 significant bits, exact, and 128 columns are a group of
 //          scale 1.  For fp32 outputs and the loss.
 //  scaled  (forward) One accumulator for the whole sum.  Integer formats:
-//          What 2^(11 - E), its scale and then its value rounded to 11 bits (E
-//          the binade of the matrix's largest scale, so the largest operand is
-//          15 x 2^12): two roundings of at most 2^-11 per product, well inside
+//          What 2^(14 - E), its scale and then its value rounded to 11 bits (E
+//          the binade of M, the matrix's largest |s| max(z, 15 - z), int3 4 |s|:
+//          operands stay below 2^15 whatever byte a zero-point is): two roundings of at most 2^-11 per product, well inside
 //          the 2^-8 of the 16-bit outputs it serves, and it spares the adding
 //          of groups, which bounds the exact kind (128 FMAs of 8 warps per
 //          64-wide step).  NVFP4 values are exact.
@@ -62,8 +62,8 @@
 //          leave it: operands as in the scaled kind, D beside a power of two
 //          per token.  A is read MN-major: a weight row's 64 columns are
 //          contiguous in the records and in the operand.
-// A scale loses bits below 2^-25 of the matrix's largest, by at most 2^-32 of
-// that, a token's or gradient's value below 2^-28 of its bound, by at most
+// A scale loses bits below 2^-28 M, by at most 2^-39 M (times a code less its
+// zero-point, and the product 2^-39 M again: 2^-31 M in all), a token's or gradient's value below 2^-28 of its bound, by at most
 // 2^-39 of that.
 //
 // The order of the columns in an operand row is the one that costs least to
@@ -460,7 +460,7 @@ __host__ __device__ constexpr uint32_t rw_half2(float v) {   // v: a power of tw
 
 // Decodes a step into the thread's operand row: 128 bytes at `row`, 16-byte
 // units swizzled by x7, columns in rows_column's order.  SCALE: times the
-// group's scale as f16 (integer formats: s winv, winv = 2^(11 - E)); the exact
+// group's scale as f16 (integer formats: s winv, winv = 2^(14 - E)); the exact
 // kind's codes of records that are not there meet tokens of 0, or belong to
 // rows without an output.
 template <int FMT, bool SCALE>
@@ -1065,7 +1065,7 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                 int64_t o;
                 if (SCALE && FMT != TQ_NVFP4_G16 && w.t.e != we) {
                     we = w.t.e;
-                    inv = pow2_of(rows_wmax(a, we, lane)).inv * 2048.f;
+                    inv = pow2_of(rows_wmax(a, we, lane)).inv * 16384.f;
                 }
                 if constexpr (BWD) {
                     o = a.o_begin + (tid >> 1);
@@ -1140,8 +1140,8 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
             auto finish = [&](auto get) {
                 if constexpr (BWD) {
                     const float wm = rows_wmax(a, t.e, lane);
-                    // integer formats: the operands were What 2^(11 - E); NVFP4: What / g (gated: g is in D)
-                    float ws = FMT != TQ_NVFP4_G16 ? pow2_of(wm).p * 4.8828125e-04f
+                    // integer formats: the operands were What 2^(14 - E); NVFP4: What / g (gated: g is in D)
+                    float ws = FMT != TQ_NVFP4_G16 ? pow2_of(wm).p * 6.103515625e-05f
                                : a.mode == ROWS_GATED_BWD ? 1.f : __ldg(a.gs[0] + t.e);
                     if (a.mode == ROWS_PROB) ws *= 1.f / ROWS_PROB_SCALE;
                     rw_grad<FMT, CW>(a, t, p, rows_bound_wm<FMT>(a, t.e, wm), ws, get);
@@ -1161,7 +1161,7 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                 }
             };
             // A column's factor: the power of two beside its token, and what the
-            // weights still lack: 2^(E - 11) or, NVFP4, the global scale (by
+            // weights still lack: 2^(E - 14) or, NVFP4, the global scale (by
             // row: see gs).
             auto factors = [&](float ws) {
                 const int r0 = t.row0 + p.col0, tid = p.warp4 * 32 + lane;
@@ -1229,7 +1229,7 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                 float gs = 1.f;   // NVFP4, forward: the global scale of the lane's projection
                 if constexpr (!BWD) {
                     if (FMT == TQ_NVFP4_G16) gs = __ldg((a.projections == 2 && lane >= 16 ? a.gs[1] : a.gs[0]) + t.e);
-                    factors(FMT == TQ_NVFP4_G16 ? 1.f : pow2_of(rows_wmax(a, t.e, lane)).p * 4.8828125e-04f);   // 2^(E - 11)
+                    factors(FMT == TQ_NVFP4_G16 ? 1.f : pow2_of(rows_wmax(a, t.e, lane)).p * 6.103515625e-05f);   // 2^(E - 14)
                 }
                 finish([&](int c0, float (&v)[32]) {
                     uint32_t w[32];

@@ -375,7 +375,8 @@ tq_status tq_gemm_nvfp4(const uint8_t* x_packed, const uint8_t* x_scales_mma, co
  * fp32 scale one by one: |y - What x| <= (I/16 + G + 32) 2^-22 sum |What x| + r
  * (G = groups per row).  bf16 y of the integer formats: weights of 11
  * significant bits, |y - What x| <= (2^-10 + (I/16 + 32) 2^-22) sum |What x| +
- * 2^-32 s sum |x| + r, s the matrix's largest scale.  Few rows (at most 32
+ * 2^-31 M sum |x| + r, M the matrix's largest |s| max(z, 15 - z) (int3: 4 |s|;
+ * a zero-point is any byte, as for tq_dequant).  Few rows (at most 32
  * per matrix on average; with many or large matrices at most 4 to 16, by
  * format) take the zero-point from the groups' sums, whatever y's
  * type: |y - What x| <= (I/16 + 2 G + 32) 2^-22 sum s (q + z) |x| + r (int3:
@@ -386,9 +387,8 @@ tq_status tq_gemm_nvfp4(const uint8_t* x_packed, const uint8_t* x_scales_mma, co
  * the records are constants and have no gradient.  The operands are rounded
  * to 11 significant bits (f16; the scales and dy beside powers of two): per
  * element, before the rounding to bf16, |dx - What^T dy| <= (2^-10 + (O/16 +
- * 32) 2^-22) sum |What dy| + 2^-32 s sum |dy| + 2^-39 max|dy[t]| sum |What|,
- * s the matrix's largest scale (the last two are for values far below the
- * largest). */
+ * 32) 2^-22) sum |What dy| + 2^-31 M sum |dy| + 2^-39 max|dy[t]| sum |What|
+ * (the last two are for values far below the largest; NVFP4: without M's). */
 typedef struct tq_records {
     const uint8_t* packed;
     const void* scales;

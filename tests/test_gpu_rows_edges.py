@@ -1,0 +1,117 @@
+"""Row products at the ends of their types' ranges: zero-points of any byte,
+gates, tokens and norms far from one, tiles of the vocabulary that nothing is
+left of."""
+import pytest
+import torch
+
+import rows_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+tq = pytest.importorskip("group_scale_search_b200")
+
+BF16, FP32 = 2.0 ** -8, 2.0 ** -24
+FMTS = list(ref.FMT)
+INT4 = [f for f in FMTS if f.startswith("int4")]
+FEW_OR_NOT = [5, 90]   # rows for the few-token kernel, and for the other
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    tq.lib()
+
+
+def normal(R, n, seed, scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn((R, n), generator=gen, dtype=torch.float64) * scale).to(torch.bfloat16).cuda()
+
+
+def largest(*ws):
+    """M of the header's bounds: the largest |s| max(z, 15 - z), int3 4 |s| (NVFP4: the largest |What|)."""
+    m = 0.0
+    for w in ws:
+        if w.fmt == "nvfp4":
+            k = w.dense().abs().max()
+        elif w.fmt == "int3":
+            k = 4 * w.scales.abs().max()
+        else:
+            z = w.zeros.double()
+            k = (w.scales.double().abs() * torch.maximum(z, 15 - z)).max()
+        m = max(m, k.item())
+    return m
+
+
+def scaled(w, by):
+    """The same records with values `by` times as large."""
+    if w.fmt == "nvfp4":
+        w.glob *= by
+    else:
+        w.scales *= by
+    return w
+
+
+def check_all(g, u, x, d, act="silu"):
+    """Every product and gradient of one pair of matrices against 64 bits."""
+    R, (_, O, I) = x.shape[0], g.shape
+    few, fmt = R <= 32, g.fmt
+    gh, uh = g.handle(tq), u.handle(tq)
+    M = largest(g, u)
+    # 2^-31 M sum |x| is 2^-32 times 2 M as rows_ref takes it; of the gated bound's 15 smax, M
+    z, err = ref.either(x, g, 0, "few" if few else None)
+    ref.check(tq.tq_dequant_matmul(x, gh, out_dtype=torch.float32), z, err, FP32)
+    if not few and fmt != "nvfp4":
+        z, err = ref.product16(x, g.dense()[0], 2 * M)
+    ref.check(tq.tq_dequant_matmul(x, gh), z, err, BF16)
+    z, err = ref.gradient(d.double(), g.dense()[0], 2.0 ** -39 * d.double().abs().amax(1, keepdim=True), 2 * M)
+    ref.check(tq.tq_dequant_matmul_backward(d, gh, I), z, err, BF16)
+    h, err = ref.gated(x, g, u, act, "few" if few else None)
+    ref.check(tq.tq_gated_ffn(x, gh, uh, act=act, out_dtype=torch.float32), h, err, FP32)
+    if not few and fmt != "nvfp4":
+        h, err = ref.gated(x, g, u, act, 2 * M)
+    ref.check(tq.tq_gated_ffn(x, gh, uh, act=act), h, err, BF16)
+    dx, err = ref.gated_grad(d, x, g, u, act, 2 * M, fmt == "nvfp4", few=few)
+    got = tq.tq_gated_ffn_backward(d, x, gh, uh, act=act)
+    ref.check(got, dx, err, BF16)
+    assert (got.double() - dx).norm() <= 0.01 * dx.norm()   # (rounding does far less than the bound's worst case)
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("zero", [15, 16, 17, 31, 255])
+@pytest.mark.parametrize("fmt", INT4)
+def test_any_zero_point(fmt, zero, R):
+    """A byte is a byte: a zero-point outside the codes' range, in groups whose
+    scale is the matrix's largest, just below a power of two."""
+    O, I = 150, 264
+    g, u = ref.Weights(fmt, 1, O, I, 1, "cuda"), ref.Weights(fmt, 1, O, I, 2, "cuda")
+    for w in (g, u):
+        w.scales.clamp_(max=0.015)
+        w.scales[:, 3::40] = 0.0156   # (below 2^-6)
+        w.zeros[:, 3::40] = zero
+    check_all(g, u, normal(R, I, 3), normal(R, O, 4, 1e-3))
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("fmt", INT4)
+def test_scales_and_zeros_of_any_alignment(fmt, R):
+    """Scales that start on an element, zero-points on a byte: the same bits."""
+    O, I = 151, 264
+    g, u = ref.Weights(fmt, 1, O, I, 22, "cuda"), ref.Weights(fmt, 1, O, I, 23, "cuda")
+    x, d = normal(R, I, 24), normal(R, O, 25, 1e-3)
+
+    def run():
+        gh, uh = g.handle(tq), u.handle(tq)
+        return [tq.tq_dequant_matmul(x, gh), tq.tq_gated_ffn(x, gh, uh), tq.tq_dequant_matmul_backward(d, gh, I),
+                tq.tq_gated_ffn_backward(d, x, gh, uh)]
+
+    want = run()
+    for at_scales, at_zeros in ((1, 1), (2, 3), (0, 2), (3, 0)):
+        for w in (g, u):
+            for name, at in (("scales", at_scales), ("zeros", at_zeros)):
+                t = getattr(w, name)
+                buf = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+                view = buf[at:at + t.numel()].view(t.shape)
+                setattr(w, name, view.copy_(t))
+        for a, b in zip(want, run()):
+            assert torch.equal(a, b)
