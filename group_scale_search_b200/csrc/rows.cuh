@@ -227,13 +227,13 @@ __device__ __forceinline__ ActCoef rw_act_coef(int act) {
     return act == TQ_ACT_SILU ? ActCoef{1.f, 0.f} : ActCoef{1.5957691216057308f, 0.07135481282553f};
 }
 __device__ __forceinline__ ActGrad rw_act(ActCoef k, float g) {
-    const float g2 = g * g;
+    const float g2 = fminf(g * g, 3.0e38f);   // (SiLU multiplies it by 0, which an infinity would make a NaN)
     const float e = __expf(-g * fmaf(k.beta, g2, k.alpha));
     const float p = __fdividef(1.f, 1.f + e);
     const float q = p * __fdividef(e, 1.f + e);   // p (1 - p), without the difference's rounding
     ActGrad r;
     r.a = g * p;
-    // (where the sigmoid has reached 0 or 1, e or g^2 may have overflowed)
+    // (where the sigmoid has reached 0 or 1, e or the last factor may have overflowed)
     r.d = p + (p == 0.f || e == 0.f ? 0.f : g * q * fmaf(3.f * k.beta, g2, k.alpha));
     return r;
 }
