@@ -172,24 +172,26 @@ __global__ void __launch_bounds__(PREP_THREADS) k_rows_prep(const __grid_constan
     }
     const int64_t r = blockIdx.x;
     const RowReader d(a.src + r * a.src_ld, a.src_cols);
+    const Pow2 c = pow2_of(row_amax(d));
     if (a.dh) {
         const float amax = row_amax(RowReader(a.dh + r * a.dh_ld, a.dh_cols));
-        float s = 0.f;
+        float s = 0.f;   // of the squares beside the row's power of two: the squares alone may leave fp32
         for (int64_t i = threadIdx.x; i < d.words(); i += PREP_THREADS) {
             const uint4 v = d.word(i);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+                const float lo = __uint_as_float(w[k] << 16) * c.inv, hi = __uint_as_float(w[k] & 0xffff0000u) * c.inv;
                 s = fmaf(lo, lo, fmaf(hi, hi, s));
             }
         }
         s = block_sum(s);
-        // (a hair above the norm, whatever the sum's rounding)
-        if (threadIdx.x == 0) a.row_f[r] = amax * (sqrtf(s) * 1.0001f);
+        // (a hair above the norm, whatever the sum's rounding; and a normal
+        // number, so that what it is multiplied by later does not uncover a
+        // product rounded to 0 here)
+        if (threadIdx.x == 0) a.row_f[r] = fmaxf(amax * (sqrtf(s) * 1.0001f * c.p), 1.1754944e-38f);
     }
     if (a.f16 == nullptr) return;
-    const Pow2 c = pow2_of(row_amax(d));
     if (threadIdx.x == 0) a.f16_f[r] = c.p * 6.103515625e-05f;   // 2^-14
     const float f = c.inv * 16384.f;
     const int64_t units = (a.src_cols + 15) / 16;

@@ -163,8 +163,14 @@ __host__ __device__ __forceinline__ Pow2 pow2_of(float x) {
 // The gated backward pass stores D as f16 (dg or du) * inv * 2^14 with inv the
 // inverse power of two of a bound on |dg| and |du|: |dh| <= dmax, |u|, |g| <=
 // |x|2 |What row|2 <= |x|2 sqrt(I) wm, |act'| <= 1.13, |act(g)| <= |g|.
-__device__ __forceinline__ Pow2 gated_bound(float row_f, float wm, float root_i) {
-    return pow2_of(row_f * 1.13f * root_i * wm);
+// wm in two factors, each multiplied to a number between the gradient's size
+// and row_f's: NVFP4's two global scales together may leave fp32 where neither
+// the tokens' nor the values' size does.
+struct RowsBound {
+    float wm, g;
+};
+__device__ __forceinline__ Pow2 gated_bound(float row_f, RowsBound b, float root_i) {
+    return pow2_of(row_f * b.wm * (1.13f * root_i) * b.g);
 }
 
 // ------------------------------------------------------------------ device helpers
@@ -269,11 +275,10 @@ __device__ __forceinline__ float rows_wmax(const RowsArgs& a, int e, int lane) {
 // the matrix's projections (NVFP4: D carries each projection's global scale,
 // so both scales' product stands in it).
 template <int FMT>
-__device__ __forceinline__ float rows_bound_wm(const RowsArgs& a, int e, float wm) {
-    if (FMT != TQ_NVFP4_G16) return wm;
-    float b = wm * 6.f;   // (E2M1's largest)
-    if (a.projections == 2) b *= fabsf(__ldg(a.gs[0] + e)) * fabsf(__ldg(a.gs[1] + e));
-    return b;
+__device__ __forceinline__ RowsBound rows_bound_wm(const RowsArgs& a, int e, float wm) {
+    if (FMT != TQ_NVFP4_G16) return {wm, 1.f};
+    if (a.projections != 2) return {wm * 6.f, 1.f};   // (6: E2M1's largest)
+    return {wm * 6.f * fabsf(__ldg(a.gs[0] + e)), fabsf(__ldg(a.gs[1] + e))};
 }
 
 }  // namespace tq

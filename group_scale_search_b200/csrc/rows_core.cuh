@@ -668,7 +668,7 @@ __device__ __forceinline__ void rw_store(const RowsArgs& a, const RwTile& t, con
 // rows of the same f.  One shuffle per two columns gives the lower lanes g
 // and u of the even column and the upper lanes those of the odd one.
 template <int CW, class Get>
-__device__ __forceinline__ void rw_gated(const RowsArgs& a, const RwTile& t, const RwPlace& p, float bound_wm,
+__device__ __forceinline__ void rw_gated(const RowsArgs& a, const RwTile& t, const RwPlace& p, RowsBound bound_wm,
                                          Get get) {
     const int up = p.lane >> 4, tid = p.warp4 * 32 + p.lane;
     const int64_t f = static_cast<int64_t>(t.m) * 64 + p.warp4 * 16 + (p.lane & 15);
@@ -821,7 +821,7 @@ __device__ __forceinline__ void rw_prob(const RowsArgs& a, const RwTile& t, cons
 // dx (or its partial sums) of 128 columns: a lane is a column, in the
 // operand's order.
 template <int FMT, int CW, class Get>
-__device__ __forceinline__ void rw_grad(const RowsArgs& a, const RwTile& t, const RwPlace& p, float bound_wm,
+__device__ __forceinline__ void rw_grad(const RowsArgs& a, const RwTile& t, const RwPlace& p, RowsBound bound_wm,
                                         float wscale, Get get) {
     const int64_t j = static_cast<int64_t>(t.m) * 128 + rows_column(FMT, p.warp4 * 32 + p.lane);
     const int r0 = t.row0 + p.col0, rows = min(t.row_end - r0, CW), n = j < a.I ? rows : 0;
@@ -1149,14 +1149,15 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                     rw_store<CW>(a, t, p, get);
                 } else if (KIND == ROWS_SCALED) {   // (the losses are for the exact kind)
                     rw_gated<CW>(a, t, p,
-                                 a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : 0.f, get);
+                                 a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : RowsBound{},
+                                 get);
                 } else if (a.mode == ROWS_LOSS) {
                     rw_loss<CW>(a, t, p, get);
                 } else if (a.mode == ROWS_PROB) {
                     rw_prob<CW>(a, t, p, get);
                 } else {
-                    const float wm =
-                        a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : 0.f;
+                    const RowsBound wm =
+                        a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : RowsBound{};
                     rw_gated<CW>(a, t, p, wm, get);
                 }
             };

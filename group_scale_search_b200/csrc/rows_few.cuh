@@ -409,7 +409,7 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
         };
         if (gated) {
             const bool grad = a.mode == ROWS_GATED_BWD;
-            const float wm = grad ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : 0.f;
+            const RowsBound wm = grad ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : RowsBound{};
             for (int v = gtid; v < 16 * 8 * NB; v += ks * 32) {
                 const int tok = v >> 4, r = v & 15;
                 const int64_t f = static_cast<int64_t>(t.m) * 16 + r;

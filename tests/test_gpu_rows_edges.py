@@ -138,3 +138,18 @@ def test_gates_whose_square_is_no_float(fmt, act, R):
     z, err = ref.product16(x, Wg, 2 * largest(g, u)) if R > 32 and fmt != "nvfp4" else ref.either(x, g, 0, "few" if R <= 32 else None)
     step = torch.where(z.abs() <= err, (d.double() * (x.double() @ u.dense()[0].T)).abs(), 0.0)
     check_all(g, u, x, d, act, 1.26 * (step.norm() * torch.linalg.matrix_norm(Wg, 2)).item())
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [1e-27, 1e-24, 1e20, 1e26])
+def test_gated_gradient_of_rows_whose_square_is_no_float(fmt, size, R):
+    """Tokens whose squares leave fp32, weights that bring gate and up back to
+    about one."""
+    O, I = 140, 200
+    g, u = (scaled(ref.Weights(fmt, 1, O, I, s, "cuda"), 1 / size) for s in (10, 11))
+    x, d = normal(R, I, 12, size), normal(R, O, 13, 1e-3)
+    dx, err = ref.gated_grad(d, x, g, u, "silu", 2 * largest(g, u), fmt == "nvfp4", few=R <= 32)
+    got = tq.tq_gated_ffn_backward(d, x, g.handle(tq), u.handle(tq))
+    ref.check(got, dx, err, BF16)
+    assert (got.double() - dx).norm() <= 0.01 * dx.norm()   # (rounding does far less than the bound's worst case)
