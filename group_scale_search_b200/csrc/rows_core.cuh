@@ -1219,7 +1219,7 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                     uint32_t w[32];
                     rw_ld32(tlane + static_cast<uint32_t>(NT * b + c0), w);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]) * p.xf[c0 + i] * gs;
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]) * gs * p.xf[c0 + i];   // (gs first: see below)
                 });
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 if (lane == 0) rw_arrive<CG>(acc_empty_l + 8 * b);
@@ -1238,8 +1238,10 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         v[i] = __uint_as_float(w[i]);
-                        if (!BWD) v[i] *= p.xf[c0 + i];
+                        // (the global scale first: with the tokens' power of
+                        // two alone the sum may overflow)
                         if (!BWD && FMT == TQ_NVFP4_G16) v[i] *= gs;
+                        if (!BWD) v[i] *= p.xf[c0 + i];
                     }
                 });
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

@@ -204,7 +204,9 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
     using F = FewFmt<FMT>;
     constexpr int PD = 2;
     constexpr bool INT = FMT != TQ_NVFP4_G16;
-    constexpr float UNIT = INT ? 16777216.f : 1.f;   // the fields' 2^-24
+    // the fields' 2^-24, half of it to the sums and half to the tokens' power of
+    // two, which goes up to 2^112
+    constexpr float HALF_UNIT = INT ? 4096.f : 1.f;
     constexpr int VALS = 2 * NB * 4 * 32;   // sums of a warp: 2 tiles of 16 rows x 8 NB tokens
     extern __shared__ float few_smem[];
     float* red = few_smem;                                             // [2][FEW_WARPS][VALS]
@@ -414,12 +416,10 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                 const int tok = v >> 4, r = v & 15;
                 const int64_t f = static_cast<int64_t>(t.m) * 16 + r;
                 if (tok < t.n && f < a.O) {
-                    const float sx = few_prepared(a.row_x + t.row0 + tok) * UNIT;
-                    float g = sum(0, tok, r) * sx, u = sum(1, tok, r) * sx;
-                    if (FMT == TQ_NVFP4_G16) {
-                        g *= __ldg(a.gs[0] + t.e);
-                        u *= __ldg(a.gs[1] + t.e);
-                    }
+                    const float sx = few_prepared(a.row_x + t.row0 + tok) * HALF_UNIT;
+                    // (NVFP4: the global scale before the tokens' power of two, with which alone the sum may overflow)
+                    const float g = sum(0, tok, r) * (INT ? HALF_UNIT : __ldg(a.gs[0] + t.e)) * sx;
+                    const float u = sum(1, tok, r) * (INT ? HALF_UNIT : __ldg(a.gs[1] + t.e)) * sx;
                     const int64_t tr = t.row0 + tok;
                     const ActGrad w = rw_act(rw_act_coef(a.act), g);
                     if (!grad) {
@@ -439,8 +439,9 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                 const int tok = v >> 5, r = v & 31;
                 const int64_t o = a.o_begin + static_cast<int64_t>(t.m) * 32 + r;
                 const bool live = tok < t.n && o < a.o_end;
-                float z = live ? sum(r >> 4, tok, r & 15) * (few_prepared(a.row_x + t.row0 + tok) * UNIT) : 0.f;
-                if (FMT == TQ_NVFP4_G16) z *= __ldg(a.gs[0] + t.e);
+                const float z = live ? sum(r >> 4, tok, r & 15) * (INT ? HALF_UNIT : __ldg(a.gs[0] + t.e)) *
+                                           (few_prepared(a.row_x + t.row0 + tok) * HALF_UNIT)
+                                     : 0.f;
                 if (a.mode == ROWS_STORE) {
                     if (live) rows_put(a.y, (t.row0 + tok) * a.ldy + o, a.y_bf16, z);
                 } else if (a.mode == ROWS_PROB) {

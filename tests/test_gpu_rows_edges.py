@@ -153,3 +153,26 @@ def test_gated_gradient_of_rows_whose_square_is_no_float(fmt, size, R):
     got = tq.tq_gated_ffn_backward(d, x, g.handle(tq), u.handle(tq))
     ref.check(got, dx, err, BF16)
     assert (got.double() - dx).norm() <= 0.01 * dx.norm()   # (rounding does far less than the bound's worst case)
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tokens_near_the_largest(fmt, R):
+    """Tokens up to 2^119, weights that bring the products back."""
+    O, I = 70, 200
+    x = normal(R, I, 16, 2.0 ** 117)
+    few = "few" if R <= 32 else None
+    w = scaled(ref.Weights(fmt, 1, O, I, 14, "cuda"), 2.0 ** -100)
+    z, err = ref.either(x, w, 0, few)
+    ref.check(tq.tq_dequant_matmul(x, w.handle(tq), out_dtype=torch.float32), z, err, FP32)
+    if fmt != "nvfp4" and few is None:
+        z, err = ref.product16(x, w.dense()[0], 2 * largest(w))
+    ref.check(tq.tq_dequant_matmul(x, w.handle(tq)), z, err, BF16)
+    scaled(w, 2.0 ** -14)   # products of about ten
+    h, err = ref.gated(x, w, w, "silu", few)
+    ref.check(tq.tq_gated_ffn(x, w.handle(tq), w.handle(tq), out_dtype=torch.float32), h, err, FP32)
+    labels = torch.arange(R, device="cuda") % O
+    want, lse64, err = ref.head_loss(x, w, labels, few is not None)
+    loss, lse = tq.tq_head_loss(x, w.handle(tq), labels)
+    ref.check(lse, lse64, err, FP32)
+    ref.check(loss, want, err, FP32)
