@@ -781,12 +781,13 @@ __device__ __forceinline__ void rw_loss(const RowsArgs& a, const RwTile& t, cons
         p.red[p.warp4 * CW + c0 + p.lane] = rw_columns<false>(v, p.lane);
     }
     rw_bar(p.bar, 128);
-    const bool none = a.o_begin + static_cast<int64_t>(t.m) * 128 >= a.o_end;   // (the pair's second tile may be past the end)
     for (int c = tid; c < n; c += 128) {
         float s = p.red[c];
 #pragma unroll
         for (int w = 1; w < 4; ++w) s += p.red[w * CW + c];
-        a.part[static_cast<int64_t>(t.m) * a.R + r0 + c] = make_float2(none ? -3.0e38f : p.colf[c], s);
+        // (no sum: the pair's second tile may be past the end, and all of a
+        // tile's logits -inf; its 0 above is no largest that others join)
+        a.part[static_cast<int64_t>(t.m) * a.R + r0 + c] = make_float2(s == 0.f ? -3.0e38f : p.colf[c], s);
     }
 }
 

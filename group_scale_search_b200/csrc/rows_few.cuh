@@ -461,7 +461,8 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
                     float s = live ? rw_exp(z - m) : 0.f;
 #pragma unroll
                     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(FULL, s, k);
-                    if (r == 0) a.part[static_cast<int64_t>(t.m) * a.R + tr] = make_float2(m, s);
+                    // (no sum: all of the tile's logits are -inf, and the 0 above is no largest that others join)
+                    if (r == 0) a.part[static_cast<int64_t>(t.m) * a.R + tr] = make_float2(s == 0.f ? -3.0e38f : m, s);
                 }
             }
         }

@@ -176,3 +176,33 @@ def test_tokens_near_the_largest(fmt, R):
     loss, lse = tq.tq_head_loss(x, w.handle(tq), labels)
     ref.check(lse, lse64, err, FP32)
     ref.check(loss, want, err, FP32)
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("fmt", ["int3", "int4g64"])
+def test_a_tile_of_the_vocabulary_at_minus_infinity(fmt, R):
+    """Entries masked by an infinite scale, whole tiles of them, beside logits
+    far below zero: the sum is that of the others."""
+    V, I = 700, 64
+    w = ref.Weights(fmt, 1, V, I, 17, "cuda")
+    w.packed.zero_()   # codes 0: every value -4 or -15 scales
+    if w.zeros is not None:
+        w.zeros.fill_(15)
+    w.scales[:] = (torch.rand(1, V, 1, generator=torch.Generator().manual_seed(18)) + 1).cuda()
+    keep = torch.ones(V, dtype=torch.bool, device="cuda")
+    keep[:256] = False
+    keep[512:640] = False
+    w.scales[0, ~keep] = float("inf")
+    x = torch.rand((R, I), generator=torch.Generator().manual_seed(19)).add_(0.5).to(torch.bfloat16).cuda()
+    labels = torch.full((R,), 300, device="cuda")
+    one = ref.Weights.__new__(ref.Weights)
+    one.__dict__.update(w.__dict__)
+    one.scales = w.scales[:, keep]
+    one.zeros = None if w.zeros is None else w.zeros[:, keep]
+    one.packed = w.packed.view(V, -1)[keep].reshape(-1)
+    one.shape = (1, int(keep.sum()), I)
+    want, lse64, err = ref.head_loss(x, one, labels - 256, R <= 32)
+    assert lse64.max() < -100
+    loss, lse = tq.tq_head_loss(x, w.handle(tq), labels)
+    ref.check(lse, lse64, err, FP32)
+    ref.check(loss, want, err, FP32)
