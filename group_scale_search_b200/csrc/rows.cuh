@@ -15,10 +15,14 @@ enum RowsMode {
     ROWS_GATED = 1,      // h = act(g) u
     ROWS_GATED_BWD = 2,  // D = (dh u act'(g), dh act(g)), f16, scaled by a power of two per token
     ROWS_LOSS = 3,       // per token and tile: max z, sum exp(z - max); the label's z
-    ROWS_PROB = 4        // D = exp(z - lse) - [o = label], f16, times 2^10
+    ROWS_PROB = 4        // D = exp(z - lse) - [o = label], f16, times 2^13
 };
 
-constexpr float ROWS_PROB_SCALE = 1024.f;   // of ROWS_PROB's D
+// Of ROWS_PROB's D: probabilities keep 11 bits down to 2^-27 and vanish below
+// 2^-38; they may be up to 8, since a logit computed by another kernel than the
+// lse's may be above it where logits are so large that fp32 holds them to one or
+// two only.
+constexpr float ROWS_PROB_SCALE = 8192.f;
 // Partial maxima of a matrix's values: enough blocks for one matrix, few of each
 // where there are many.
 __host__ __device__ __forceinline__ int rows_wmax_parts(int E) { return E <= 2 ? 64 : E >= 32 ? 4 : 128 / E; }

@@ -791,7 +791,7 @@ __device__ __forceinline__ void rw_loss(const RowsArgs& a, const RwTile& t, cons
     }
 }
 
-// D = (e^(z - lse) - [o is the label]) 2^10 in f16; 0 for a token without one.
+// D = (e^(z - lse) - [o is the label]) 2^13 in f16; 0 for a token without one.
 template <int CW, class Get>
 __device__ __forceinline__ void rw_prob(const RowsArgs& a, const RwTile& t, const RwPlace& p, Get get) {
     const int64_t o = a.o_begin + static_cast<int64_t>(t.m) * 128 + p.warp4 * 32 + p.lane;

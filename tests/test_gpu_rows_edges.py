@@ -1,6 +1,8 @@
 """Row products at the ends of their types' ranges: zero-points of any byte,
 gates, tokens and norms far from one, tiles of the vocabulary that nothing is
 left of."""
+import math
+
 import pytest
 import torch
 
@@ -206,3 +208,25 @@ def test_a_tile_of_the_vocabulary_at_minus_infinity(fmt, R):
     loss, lse = tq.tq_head_loss(x, w.handle(tq), labels)
     ref.check(lse, lse64, err, FP32)
     ref.check(loss, want, err, FP32)
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gradient_of_small_probabilities(fmt, R):
+    """Probabilities of about 2^-34.5 (the rest of the sum is elsewhere) and a
+    label whose own row is zero: the gradient is theirs alone.  Each is held to
+    2^-11 of itself or 2^-38, and |err W| <= |err| |W|, the largest singular
+    value."""
+    V, I = 300, 64
+    w = ref.Weights(fmt, 1, V, I, 20, "cuda")
+    w.scales[0, V - 1] = 0
+    x = normal(R, I, 21, 0.1)
+    labels = torch.full((R,), V - 1, device="cuda")
+    lse = torch.full((R,), 34.5 * math.log(2), device="cuda")
+    W = w.dense()[0]
+    p = torch.exp(x.double() @ W.T - lse.double()[:, None])
+    want = p[:, :-1] @ W[:-1]
+    err = ((p * 2.0 ** -11).norm(dim=1) + V ** 0.5 * 2.0 ** -38) * torch.linalg.matrix_norm(W, 2)
+    got = tq.tq_head_loss_backward(torch.ones(R, device="cuda"), x, w.handle(tq), labels, lse).double()
+    off = (got - want).norm(dim=1)
+    assert (off <= err * (1 + BF16) + 2.0 ** -9 * want.norm(dim=1)).all(), (off / want.norm(dim=1)).max()
