@@ -520,6 +520,7 @@ static tq_status check_records(const tq_records* W, const char* name) {
     TQ_REQUIRE(W->fmt == TQ_NVFP4_G16 || !W->global_scale, "%s: global_scale is for NVFP4 only", name);
     TQ_REQUIRE(W->fmt == TQ_NVFP4_G16 || (reinterpret_cast<uintptr_t>(W->scales) & 3u) == 0,
                "%s: scales not 4-byte aligned", name);
+    TQ_REQUIRE((reinterpret_cast<uintptr_t>(W->global_scale) & 3u) == 0, "%s: global_scale not 4-byte aligned", name);
     TQ_REQUIRE(W->n_mat >= 1 && W->O >= 1 && W->I >= 1, "%s: empty or negative shape", name);
     TQ_REQUIRE(W->n_mat <= ROWS_MAX_MATS, "%s: more than %d matrices", name, ROWS_MAX_MATS);
     TQ_REQUIRE(W->O < (int64_t(1) << 30) && W->I < (int64_t(1) << 30) &&
@@ -1017,6 +1018,8 @@ TQ_API tq_status tq_head_loss(const tq_records* W, const tq_mat* X, const int64_
     if (X->rows == 0) return TQ_OK;
     TQ_REQUIRE(labels && loss && lse, "tq_head_loss: null pointer");
     TQ_REQUIRE((reinterpret_cast<uintptr_t>(labels) & 7u) == 0, "tq_head_loss: labels not 8-byte aligned");
+    TQ_REQUIRE(((reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(lse)) & 3u) == 0,
+               "tq_head_loss: loss or lse not 4-byte aligned");
     RowsArgs a = rows_args(W, nullptr, X->rows, nullptr);
     const LossSpace l = loss_space(workspace, a);
     ROWS_TRY(check_workspace(workspace, workspace_bytes, l.bytes, "tq_head_loss"));
@@ -1055,6 +1058,8 @@ TQ_API tq_status tq_head_loss_backward(const tq_records* W, const tq_mat* X, con
     if (X->rows == 0) return TQ_OK;
     TQ_REQUIRE(labels && lse && dloss, "tq_head_loss_backward: null pointer");
     TQ_REQUIRE((reinterpret_cast<uintptr_t>(labels) & 7u) == 0, "tq_head_loss_backward: labels not 8-byte aligned");
+    TQ_REQUIRE(((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(dloss)) & 3u) == 0,
+               "tq_head_loss_backward: lse or dloss not 4-byte aligned");
     RowsArgs a = rows_args(W, nullptr, X->rows, nullptr);
     const int64_t piece = loss_piece(a.R, W->O);
     const BackwardSpace b = backward_space(a, true, piece, false, piece < W->O, workspace);
