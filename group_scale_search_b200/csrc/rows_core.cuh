@@ -87,6 +87,8 @@
 
 namespace tq {
 
+// Waits that gave up, of this format: each including file has a counter of its
+// own, and so rw_take_timeouts() below is static.
 static __device__ unsigned g_rw_timeouts = 0;
 
 constexpr int RW_A_BYTES = 128 * 128;
@@ -1351,7 +1353,7 @@ tq_status rw_launch_fmt(const RowsArgs& a, const RowsLaunch& l, cudaStream_t st)
     return rw_launch_nt<FMT, ROWS_SCALED>(a, l, st);
 }
 
-inline bool rw_take_timeouts() {
+static bool rw_take_timeouts() {
     unsigned n = 0;
     if (cudaMemcpyFromSymbol(&n, g_rw_timeouts, sizeof(n)) != cudaSuccess || n == 0) return false;
     const unsigned zero = 0;

@@ -38,3 +38,21 @@ def test_what_a_running_grid_writes_is_not_read_as_read_only_data():
         assert not any(re.search(rf"\b{n}\b", arg) for n in made), arg
     before = text[text.index("k_rows_few(const"):text.index("grid_wait();", text.index("k_rows_few(const"))]
     assert not any(re.search(rf"\b{n}\b", before) for n in made)
+
+
+def test_a_counter_of_one_translation_unit_is_read_by_its_own_function():
+    """rows_core.cuh is compiled once per format, each with a counter of
+    given-up waits of its own (a static variable).  A host function in it that
+    reads the counter must be static too: of one with external linkage the
+    linker may keep a single copy, which reads one format's counter for all."""
+    text = code("rows_core.cuh")
+    own = re.findall(r"^static (?:__device__ |std::atomic<\w+> )\w*\s*(\w+)\s*[={]", text, flags=re.M)
+    assert "g_rw_timeouts" in own
+    found = 0
+    # functions at the file's left margin, up to the closing brace there
+    for m in re.finditer(r"^(?!template|namespace|struct|constexpr|enum)([^\n;{]*\([^;{]*\))\s*\{\n(.*?)^\}", text, flags=re.S | re.M):
+        if "__device__" in m[1] or "__global__" in m[1] or not any(re.search(rf"\b{n}\b", m[2]) for n in own):
+            continue
+        found += 1
+        assert m[1].startswith("static "), m[1]
+    assert found
