@@ -88,8 +88,11 @@
 namespace tq {
 
 // Waits that gave up, of this format: each including file has a counter of its
-// own, and so rw_take_timeouts() below is static.
+// own, and so rw_take_timeouts() below is static.  Reading it costs tq_sync a
+// copy, so it is read once a kernel of the format has been launched (or
+// captured: a graph may run it any time later).
 static __device__ unsigned g_rw_timeouts = 0;
+static std::atomic<bool> g_rw_launched{false};
 
 constexpr int RW_A_BYTES = 128 * 128;
 
@@ -1332,6 +1335,7 @@ tq_status rw_launch(const RowsArgs& a, const RowsLaunch& l, cudaStream_t st) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = C::CG == 2 ? 1 : 0;
+    g_rw_launched.store(true, std::memory_order_relaxed);
     cudaLaunchKernelEx(&cfg, k_rows<FMT, NT, KIND>, *l.map, a);
     return check_launch("row products");
 }
@@ -1354,6 +1358,7 @@ tq_status rw_launch_fmt(const RowsArgs& a, const RowsLaunch& l, cudaStream_t st)
 }
 
 static bool rw_take_timeouts() {
+    if (!g_rw_launched.load(std::memory_order_relaxed)) return false;
     unsigned n = 0;
     if (cudaMemcpyFromSymbol(&n, g_rw_timeouts, sizeof(n)) != cudaSuccess || n == 0) return false;
     const unsigned zero = 0;
