@@ -671,15 +671,16 @@ __device__ __forceinline__ void rw_store(const RowsArgs& a, const RwTile& t, con
 
 // Gated: lanes 0-15 of a warp hold gate rows f .. f + 15, lanes 16-31 the up
 // rows of the same f.  One shuffle per two columns gives the lower lanes g
-// and u of the even column and the upper lanes those of the odd one.
-template <int CW, class Get>
+// and u of the even column and the upper lanes those of the odd one.  GRAD: the
+// gated backward pass may ask for D instead of h (in the scaled kind alone).
+template <int CW, bool GRAD, class Get>
 __device__ __forceinline__ void rw_gated(const RowsArgs& a, const RwTile& t, const RwPlace& p, RowsBound bound_wm,
                                          Get get) {
     const int up = p.lane >> 4, tid = p.warp4 * 32 + p.lane;
     const int64_t f = static_cast<int64_t>(t.m) * 64 + p.warp4 * 16 + (p.lane & 15);
     const int r0 = t.row0 + p.col0, rows = min(t.row_end - r0, CW), n = f < a.O ? rows : 0;
     const ActCoef k = rw_act_coef(a.act);
-    const bool grad = a.mode == ROWS_GATED_BWD;
+    const bool grad = GRAD && a.mode == ROWS_GATED_BWD;
     const float s0 = grad && a.gs[0] ? __ldg(a.gs[0] + t.e) : 1.f, s1 = grad && a.gs[1] ? __ldg(a.gs[1] + t.e) : 1.f;
     if (grad) {
         for (int c = tid; c < CW; c += 128)
@@ -1154,17 +1155,16 @@ k_rows(const __grid_constant__ CUtensorMap map, const __grid_constant__ RowsArgs
                 } else if (a.mode == ROWS_STORE) {
                     rw_store<CW>(a, t, p, get);
                 } else if (KIND == ROWS_SCALED) {   // (the losses are for the exact kind)
-                    rw_gated<CW>(a, t, p,
-                                 a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : RowsBound{},
-                                 get);
+                    rw_gated<CW, true>(a, t, p,
+                                       a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane))
+                                                                : RowsBound{},
+                                       get);
                 } else if (a.mode == ROWS_LOSS) {
                     rw_loss<CW>(a, t, p, get);
                 } else if (a.mode == ROWS_PROB) {
                     rw_prob<CW>(a, t, p, get);
                 } else {
-                    const RowsBound wm =
-                        a.mode == ROWS_GATED_BWD ? rows_bound_wm<FMT>(a, t.e, rows_wmax(a, t.e, lane)) : RowsBound{};
-                    rw_gated<CW>(a, t, p, wm, get);
+                    rw_gated<CW, false>(a, t, p, RowsBound{}, get);
                 }
             };
             // A column's factor: the power of two beside its token, and what the
