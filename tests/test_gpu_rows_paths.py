@@ -1,6 +1,10 @@
 """Paths of the row products that only larger or more uneven calls take: every
 token-block count of the few-token kernel, its walk over several tiles, routed
 gradients whose sum is split, and the give-up path of every format."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -12,6 +16,7 @@ tq = pytest.importorskip("group_scale_search_b200")
 
 BF16, FP32 = 2.0 ** -8, 2.0 ** -24
 FMTS = list(ref.FMT)
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -176,6 +181,91 @@ def test_routed_gradients_of_a_split_sum(fmt, gated, I):
                 ds = d[s].double()
                 z, err = ref.gradient(ds, g.dense()[e], 2.0 ** -39 * ds.abs().amax(1, keepdim=True), g.largest_scale()[e])
             ref.check(out[s, :I], z, err, BF16)
+
+
+# ---------------------------------------------------------------- other ranges
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R", [30, 250])
+def test_one_matrix_and_a_range(fmt, R):
+    """offsets may be given for a single matrix too: its range of the rows."""
+    O, I = 150, 264
+    g, u = ref.Weights(fmt, 1, O, I, 25, "cuda"), ref.Weights(fmt, 1, O, I, 26, "cuda")
+    x, d = rows(R, I, 27), rows(R, O, 28, 1e-2)
+    gh, uh = g.handle(tq), u.handle(tq)
+    calls = [(O, lambda x, d, **kw: tq.tq_dequant_matmul(x, gh, **kw)), (O, lambda x, d, **kw: tq.tq_gated_ffn(x, gh, uh, **kw)),
+             (I, lambda x, d, **kw: tq.tq_dequant_matmul_backward(d, gh, I, **kw)),
+             (I, lambda x, d, **kw: tq.tq_gated_ffn_backward(d, x, gh, uh, **kw))]
+    for lo, hi in ((0, R), (3, R - 2), (7, 7)):
+        off = torch.tensor([lo, hi], dtype=torch.int32, device="cuda")
+        for n, call in calls:
+            out = torch.full((R, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            call(x, d, offsets=off, out=out)
+            assert torch.equal(out[lo:hi], call(x, d)[lo:hi])   # (a row's result does not depend on the others)
+            assert (out[:lo] == 7).all() and (out[hi:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ["int3", "int4g32", "nvfp4"])
+@pytest.mark.parametrize("R", [700, 40000])
+def test_as_many_matrices_as_there_may_be(fmt, R):
+    E, O, I = 1024, 40, 72
+    g, u = ref.Weights(fmt, E, O, I, 29, "cuda"), ref.Weights(fmt, E, O, I, 30, "cuda")
+    x, d = rows(R, I, 31), rows(R, O, 32, 1e-2)
+    expert = torch.randint(0, E, (R,), generator=torch.Generator().manual_seed(33)).sort().values.cuda()
+    off = torch.searchsorted(expert, torch.arange(E + 1, device="cuda")).to(torch.int32)
+    few = R < E
+    W, A, s = g.dense(), g.spread(), g.largest_scale()[expert, None]
+    x64 = x.double()
+    z = torch.einsum("ri,roi->ro", x64, W[expert])
+    tiny = 2.0 ** -30 * x64.abs().amax(1, keepdim=True) * W.abs().sum(2)[expert]
+    y = tq.tq_dequant_matmul(x, g.handle(tq), offsets=off, out_dtype=torch.float32)
+    size = torch.einsum("ri,roi->ro", x64.abs(), (A if few else W.abs())[expert])
+    ref.check(y, z, (I / 16 + 2 * g.G + 32) * ref.U * size + tiny, FP32)
+    d64 = d.double()
+    dx = tq.tq_dequant_matmul_backward(d, g.handle(tq), I, offsets=off)
+    size = torch.einsum("ro,roi->ri", d64.abs(), W.abs()[expert])
+    tiny = 2.0 ** -39 * d64.abs().amax(1, keepdim=True) * W.abs().sum(1)[expert] + 2.0 ** -32 * s * d64.abs().sum(1, keepdim=True)
+    ref.check(dx, torch.einsum("ro,roi->ri", d64, W[expert]), (2.0 ** -10 + (O / 16 + 32) * ref.U) * size + tiny, BF16)
+    # the block and its gradient, by the norm of what they are off
+    h = tq.tq_gated_ffn(x, g.handle(tq), u.handle(tq), offsets=off, out_dtype=torch.float32)
+    p = ref.act("silu", z)[0] * torch.einsum("ri,roi->ro", x64, u.dense()[expert])
+    assert (h.double() - p).norm() <= 1e-4 * p.norm()   # (fp32 sums of exact products)
+    db = tq.tq_gated_ffn_backward(d, x, g.handle(tq), u.handle(tq), offsets=off)
+    U_ = torch.einsum("ri,roi->ro", x64, u.dense()[expert])
+    a, da = ref.act("silu", z)
+    want = torch.einsum("ro,roi->ri", d64 * U_ * da, W[expert]) + torch.einsum("ro,roi->ri", d64 * a, u.dense()[expert])
+    assert (db.double() - want).norm() <= (BF16 + 2.0 ** -9) * want.norm()   # (its rounding, and the operands' 11 bits)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first row products are captured, each kind of kernel
+    among them, and replayed: the same bits as plain calls."""
+    code = f"""
+import sys
+sys.path[:0] = [{ROOT!r}, {os.path.join(ROOT, "tests")!r}]
+import torch
+import group_scale_search_b200 as tq, rows_ref as ref
+torch.manual_seed(1)
+x, d = (torch.randn(200, n, device="cuda").to(torch.bfloat16) for n in (256, 300))
+g, u = (ref.Weights("int4g64", 1, 300, 256, s, "cuda") for s in (1, 2))
+gh, uh = g.handle(tq), u.handle(tq)
+lab, one = torch.arange(200, device="cuda"), torch.ones(200, device="cuda")
+lse = torch.logsumexp(x.double() @ g.dense()[0].T, 1).float()
+def run(R):
+    return [tq.tq_dequant_matmul(x[:R], gh), tq.tq_dequant_matmul(x[:R], gh, out_dtype=torch.float32),
+            tq.tq_gated_ffn(x[:R], gh, uh), tq.tq_dequant_matmul_backward(d[:R], gh, 256),
+            tq.tq_gated_ffn_backward(d[:R], x[:R], gh, uh), tq.tq_head_loss(x[:R], gh, lab[:R])[0],
+            tq.tq_head_loss_backward(one[:R], x[:R], gh, lab[:R], lse[:R])]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = run(5) + run(200)
+graph.replay()
+torch.cuda.synchronize()
+tq.tq_sync()
+assert all(torch.equal(a, b) for a, b in zip(outs, run(5) + run(200)))
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- giving up
