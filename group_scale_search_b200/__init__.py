@@ -20,7 +20,8 @@ Function names match the C entry points:
     tq_proxy_error(W, packed, fmt, ..) -> (num, den) per matrix
     tq_dequant_matmul(x, w), tq_gated_ffn(x, gate, up), tq_head_loss(x, w, labels)
                                        -> products of token rows with the records of a
-                                          SearchResult; each has a ..._backward
+                                          SearchResult; each has a ..._backward, which a
+                                          training step calls itself (no autograd graph)
 """
 from __future__ import annotations
 
@@ -842,7 +843,9 @@ def proxy_workspace_bytes(W: torch.Tensor, fmt: int) -> int:
 
 
 # ---------------------------------------------------------------- row products
-# Each call takes the keyword `stream` too (default: the current stream).
+# Each call takes the keyword `stream` too (default: the current stream).  None
+# records an autograd graph: outputs never require grad, whatever the tokens do,
+# and a training step calls the ..._backward functions itself.
 
 _RECORD_BYTES = {INT3_G64_SYM: 24, INT4_G128_ASYM: 64, INT4_G64_ASYM: 32, INT4_G32_ASYM: 16, NVFP4_G16: 8}
 
@@ -983,7 +986,8 @@ def tq_dequant_matmul(x: torch.Tensor, w: SearchResult, offsets: Optional[torch.
     records (packed, scales, ...) of one matrix, or of n_mat experts with
     offsets, int32 [n_mat + 1] on the GPU: rows offsets[e] .. offsets[e+1]-1
     use expert e; rows outside all of them are left as they were (undefined
-    in an `out` made here).  y: bf16 or fp32.  Up to 8 rows of one matrix in
+    in an `out` made here).  y: bf16 or fp32, without an autograd graph: its
+    gradient is tq_dequant_matmul_backward.  Up to 8 rows of one matrix in
     fp32: see also tq_dequant_gemv."""
     d, dev = _row_mat(x, "x"), x.device
     rec = _row_records(w, d.cols, "w", dev)
@@ -1024,7 +1028,7 @@ def tq_gated_ffn(x: torch.Tensor, gate: SearchResult, up: SearchResult, act: str
     """h [rows, O] = act(x Wgate^T) * (x Wup^T) in one kernel; act "silu" or
     "gelu" (tanh form).  gate and up: records of one format and shape; x,
     offsets and the output as in tq_dequant_matmul (which is the block's down
-    projection)."""
+    projection).  No autograd graph: its gradient is tq_gated_ffn_backward."""
     a = _act(act)
     d, dev = _row_mat(x, "x"), x.device
     rg, ru = _row_records(gate, d.cols, "gate", dev), _row_records(up, d.cols, "up", dev)
@@ -1072,7 +1076,8 @@ def tq_head_loss(x: torch.Tensor, w: SearchResult, labels: torch.Tensor,
     """(loss, lse), fp32 [rows]: per token the cross entropy of the packed
     head's logits What x, and their log-sum-exp, without storing the logits.
     x: bf16 [rows, I]; w: records of one [vocabulary, I] matrix; labels: int64
-    [rows], outside [0, vocabulary) where a token has none (loss 0)."""
+    [rows], outside [0, vocabulary) where a token has none (loss 0).  No
+    autograd graph: its gradient is tq_head_loss_backward."""
     d, dev = _row_mat(x, "x"), x.device
     rec = _row_records(w, d.cols, "w", dev)
     _one_matrix(rec)

@@ -444,13 +444,17 @@ bool rows_take_timeouts() {
 // Tokens per tile and splits of the sum by a model of the SMs' time in clocks:
 // waves of items x (steps x clocks of a step + clocks of an item's start and
 // end), plus the traffic of joined splits.  A step's clocks are relative ones,
-// fitted to runs with each width forced; the choice was the fastest width or
-// within 4 % of it in 40 of 42 of them.  Microseconds of 32 / 64 / 128 / 256
-// tokens a tile, 4096 columns: 1999 rows over 16 int3 experts (gated, 2048
-// outputs) 523 / 333 / 223 / 204; a gated gradient of 777 rows over them 528 /
-// 326 / 345 / 374 (128 is taken); one int4 g64 matrix of 6000 outputs, 100
-// rows 90 / 67 / 68 / 70, 300 rows 140 / 99 / 85 / 71, 1300 rows 380 / 235 /
-// 157 / 103; its loss, 200 rows 135 / 136 / 98 / 105.
+// one table for every format and kind.  Against runs with each width forced
+// (matmul in bf16 and fp32, loss, gated block and both gradients, 4096 columns,
+// all formats) the choice was within 2 % of the fastest for one matrix of 6000
+// outputs and 40 to 2500 rows (150 runs), and within 5 % for 71 of 100 runs of
+// routed rows; the others, 25 to 48 rows a matrix, took up to 1.28 times as long
+// as a width less would have, fp32 outputs of int4 g32 1.55.  Microseconds of 32
+// / 64 / 128 / 256 tokens a tile: 1999 rows over 16 int3 experts (gated, 2048
+// outputs) 481 / 298 / 189 / 173; a gated gradient of 777 rows over them 486 /
+// 290 / 309 / 338 (128 is taken); one int4 g64 matrix of 6000 outputs, 100 rows
+// 65 / 41 / 43 / 47, 300 rows 112 / 66 / 45 / 48, 1300 rows 342 / 189 / 122 /
+// 80; its loss, 300 rows 130 / 108 / 71 / 80.
 struct RowsPlan {
     int nt, splits, grid;
 };
@@ -553,18 +557,21 @@ static tq_status check_tokens(const tq_mat* X, int64_t rows, int64_t cols, const
 
 // Tokens (in blocks of 8) that the kernel for few tokens should take at a
 // time, or 0 where the tensor-memory kernel is the faster one: by the rows of
-// a matrix (routed: on average).  Microseconds, few / tensor-memory:
-//  fewer tiles than SMs: up to 32 rows.  32 rows x 8192 x 4096, int3 53 / 65,
-//    int4 g32 55 / 64, NVFP4 46 / 57; 53 rows over 2 int3 experts 24 / 56.
+// a matrix (routed: on average).  Microseconds, few / tensor-memory (the same
+// records again and again, in L2 where they fit):
+//  fewer tiles than SMs: up to 32 rows.  32 rows x 8192 x 4096, int3 32 / 43,
+//    int4 g32 35 / 44, NVFP4 24 / 33; 53 rows over 2 int3 experts 24 / 42.
 //  one matrix, more tiles: up to 16, int4 g128 up to 32.  Gated 17408 x 5120,
-//    16 rows, int3 99 / 116, g128 70 / 104, g32 107 / 119, NVFP4 70 / 92; 24
-//    rows 125 / 116, 87 / 105, 139 / 119, 91 / 92.
+//    16 rows, int3 71 / 85, g128 46 / 77, g64 58 / 85, g32 79 / 101, NVFP4 46 /
+//    68; 24 rows 88 / 86, 65 / 79, 82 / 87, 116 / 101, 66 / 69.
 //  experts: their ragged ends fill fewer blocks of 8, which the tensor-memory
-//    kernel pads for nothing.  64 x 2688 x 1856, 8 rows each, int3 155 / 160,
-//    g128 109 / 164, g64 169 / 175, g32 284 / 182, NVFP4 117 / 139; 16 rows
-//    int3 211 / 166, g128 148 / 176, NVFP4 147 / 147; 24 rows g128 182 / 178,
-//    NVFP4 186 / 145.  g32 whose rows do not end with a slice: 2 rows 180 /
-//    166, gated with a row to every third expert 201 / 246.
+//    kernel pads for nothing.  64 x 2688 x 1856, 8 rows each, int3 99 / 129,
+//    g128 70 / 141, g64 113 / 149, NVFP4 77 / 115; 12 rows int3 134 / 130, g64
+//    167 / 149; 16 rows g128 97 / 145, NVFP4 100 / 118; 24 rows g128 157 / 145,
+//    NVFP4 152 / 117.  g32 spills at 8 tokens (few_blocks_per_sm), hence its
+//    limits: 64 x 2688 x 2048, 4 rows 152 / 173, 8 rows 157 / 172 (not taken);
+//    where rows do not end with a slice, 2688 x 1856, 2 rows 169 / 160, 8 rows
+//    196 / 160.
 static int few_blocks(int32_t fmt, const RowsArgs& a) {
     const int64_t per = (a.R + a.E - 1) / a.E, tiles = a.E * tiles_of(a.O, a.projections == 2 ? 64 : 128);
     int64_t most = 32;

@@ -108,12 +108,13 @@ tq_status launch_few_int4g64(const RowsArgs& a, int nb, int mb, int grid, cudaSt
 tq_status launch_few_int4g32(const RowsArgs& a, int nb, int mb, int grid, cudaStream_t st);
 tq_status launch_few_nvfp4(const RowsArgs& a, int nb, int mb, int grid, cudaStream_t st);
 
-// Blocks per SM of that kernel.  8 tokens fit 128 registers a thread, 32 take
-// 255.  16 fit 128 without spills only where a slice is one group (int4 g128)
-// or needs no group sums (NVFP4): there two blocks, unless the grid fills no
-// more than one (17408 x 5120 int4 g128, 14 rows: 45 us against 53; 4096 x 4096,
-// 16 rows: 13 us with one, 17 with two).  The others take one (11008 x 4096
-// int4 g64, 12 rows: 29 us against 42).
+// Blocks per SM of that kernel, two of which leave a thread 128 registers, one
+// 255.  8 tokens: two (int4 g32 spills 216 bytes a thread for it, the others
+// none).  16: two where a slice is one group (int4 g128, 104 bytes) or needs no
+// group sums (NVFP4, 16 bytes), unless the grid fills no more than one (17408 x
+// 5120 int4 g128, 14 rows: 45 us against 53; 4096 x 4096, 16 rows: 13 us with
+// one, 17 with two); the other formats take one (11008 x 4096 int4 g64, 12 rows:
+// 29 us against 42).  32: one (16 to 28 bytes of int3, g64 and g32).
 __host__ __device__ constexpr bool few_two_fit(int fmt) { return fmt == TQ_INT4_G128_ASYM || fmt == TQ_NVFP4_G16; }
 inline int few_blocks_per_sm(int fmt, int nb, int64_t items, int64_t sms) {
     return nb == 1 ? 2 : nb == 2 && few_two_fit(fmt) && items > sms ? 2 : 1;

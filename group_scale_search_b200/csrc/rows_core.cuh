@@ -27,19 +27,21 @@
 // loss's, 603 / 586 / 581 for the 2048 gated rows.  At 32 tokens a tile only
 // int3, whose codes take twice the instructions: NVFP4's 3001 rows 226 / 234 /
 // 233.  NVFP4 in wider tiles is within 3 % either way: 4096 rows x 8192 x 4096
-// with two 258, their gradient 270; with four 255 and 260.)
+// with two 258, their gradient 270; with four 255 and 260.  Short runs, at full
+// clocks.)
 //
-// Measured: gated 2048 rows x 17408 x 5120 int4 g128 581 us, 1.26 PFLOP/s, where
-// shared memory is the busiest (78 %, the tensor pipe 65 %); a gradient of 8192
-// rows x 4096 x 4096 int4 g32 246 us, 1.12 PFLOP/s (decoding two scales and
-// zero-points a row and step); the loss of 1024 tokens x 65536 x 4096 680 us,
-// 0.81 PFLOP/s (exact kind: adding groups); 3001 rows over 128 NVFP4 experts of
-// 2688 x 1856 225 us, 1.7 TB/s of records: what is bound there is the decoding,
-// with few rows to a weight.
+// Measured in sustained passes, the dense ones at the power cap (1.6 to 1.8 GHz;
+// in brackets short runs): gated 2048 rows x 17408 x 5120 int4 g128 690 us, 1.06
+// PFLOP/s (581), where shared memory is the busiest (78 %, the tensor pipe 65
+// %); a gradient of 8192 rows x 4096 x 4096 int4 g32 304 us, 0.90 PFLOP/s (246;
+// decoding two scales and zero-points a row and step); the loss of 1024 tokens x
+// 65536 x 4096 700 us, 0.79 PFLOP/s (680; exact kind: adding groups); 3001 rows
+// over 128 NVFP4 experts of 2688 x 1856 224 us, 1.7 TB/s of records: what is
+// bound there is the decoding, with few rows to a weight.
 //
 // Operands are f16: 11 significant bits at the rate of bf16's 8, and powers of
 // two beside them give back the range.  The tokens are a copy in f16 with a
-// power of two per row (exact but for values 2^-17 below their row's largest).
+// power of two per row (exact but for values 2^-31 below their row's largest).
 // Three kinds (RowsKind):
 //  exact   (forward) The weights are the exact small integers v or q - z, so
 //          every product is exact; a group's sum is taken in a TMEM
@@ -63,8 +65,8 @@
 //          per token.  A is read MN-major: a weight row's 64 columns are
 //          contiguous in the records and in the operand.
 // A scale loses bits below 2^-28 M, by at most 2^-39 M (times a code less its
-// zero-point, and the product 2^-39 M again: 2^-31 M in all), a token's or gradient's value below 2^-28 of its bound, by at most
-// 2^-39 of that.
+// zero-point, and the product 2^-39 M again: 2^-31 M in all), a token's or
+// gradient's value below 2^-28 of its bound, by at most 2^-39 of that.
 //
 // The order of the columns in an operand row is the one that costs least to
 // decode (rows_column): a field of a record word is masked in place in both

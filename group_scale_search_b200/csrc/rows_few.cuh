@@ -8,8 +8,8 @@
 // takes its A operand from registers, which saves the trip of a decoded weight
 // through shared or tensor memory that tcgen05 would need, and with 8 to 32
 // tokens the tensor cores have little to do either way.  Measured: one
-// token, two 17408 x 5120 int4 g128 matrices, 31 us, 3.1 TB/s of records (the
-// tcgen05 kernel of rows_core.cuh took 93); 48 rows over 128 NVFP4 experts 83
+// token, two 17408 x 5120 int4 g128 matrices, 32 us, 3.0 TB/s of records (the
+// tcgen05 kernel of rows_core.cuh took 93); 48 rows over 128 NVFP4 experts 84
 // us, 2.8 TB/s.  Two blocks an SM are all that the registers hold, and their
 // 16 warps' instruction latency is the bound (issue 40 %).
 //

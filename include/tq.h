@@ -377,10 +377,10 @@ tq_status tq_gemm_nvfp4(const uint8_t* x_packed, const uint8_t* x_scales_mma, co
  * significant bits, |y - What x| <= (2^-10 + (I/16 + 32) 2^-22) sum |What x| +
  * 2^-31 M sum |x| + r, M the matrix's largest |s| max(z, 15 - z) (int3: 4 |s|;
  * a zero-point is any byte, as for tq_dequant).  Few rows (at most 32
- * per matrix on average; with many or large matrices at most 4 to 16, by
+ * per matrix on average; with many or large matrices at most 1 to 32, by
  * format) take the zero-point from the groups' sums, whatever y's
- * type: |y - What x| <= (I/16 + 2 G + 32) 2^-22 sum s (q + z) |x| + r (int3:
- * q + z = v + 8).  All before the rounding of bf16 outputs.  The workspace
+ * type: |y - What x| <= (I/16 + 2 G + 32) 2^-22 sum s (q + z) |x| + 2^-30
+ * max|x[t]| sum s (q + z) (int3: q + z = v + 8).  All before the rounding of bf16 outputs.  The workspace
  * (tq_dequant_matmul_workspace_bytes) holds the tokens in f16.
  *
  * tq_dequant_matmul_backward: dx[t] = What_e^T dy[t] (bf16, rows of ldx >= I);
