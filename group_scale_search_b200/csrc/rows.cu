@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(FEW_PREP_THREADS) k_few_prep(const uint16_t* x
 #pragma unroll
             for (int i = 0; i < 16; ++i) g += __half2float(__float2half_rn(v[i]));
             for (int k = 1; k < per; k *= 2) g += __shfl_xor_sync(FULL, g, k);
-            if (c < chunks && (c & (per - 1)) == 0) sums[(r * chunks + c) / per] = g * 5.9604644775390625e-08f;   // 2^-24
+            if (c < chunks && (c & (per - 1)) == 0) sums[(r * chunks + c) / per] = g * 9.765625e-04f;   // 2^-10
         }
         if (c >= chunks) continue;
         // the two units' pairs: int4 (k, k + 4) of each 8, int3 (k, k + 8) of the 16, NVFP4 (2 k, 2 k + 1)

@@ -59,7 +59,7 @@ struct RowsArgs {
     const int64_t* labels;
     const float* lse;
     const uint16_t* x_few;          // few tokens: f16 in the kernel's order, [R][slices of 128 columns][256 bytes]
-    const float* x_sums;            // integer formats: 2^-24 times the values' sum per group, [R][slices][groups of one]
+    const float* x_sums;            // integer formats: 2^-10 times the values' sum per group, [R][slices][groups of one]
     int few;                        // (host) blocks of 8 tokens that its kernel takes at a time, 0: not its call
     int few_wide, few_ks;
     float2* part;                   // ROWS_LOSS: [part_tiles][R]

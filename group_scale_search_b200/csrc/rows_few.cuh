@@ -8,7 +8,7 @@
 // takes its A operand from registers, which saves the trip of a decoded weight
 // through shared or tensor memory that tcgen05 would need, and with 8 to 32
 // tokens the tensor cores have little to do either way.  Measured: one
-// token, two 17408 x 5120 int4 g128 matrices, 32 us, 3.0 TB/s of records (the
+// token, two 17408 x 5120 int4 g128 matrices, 33 us, 2.9 TB/s of records (the
 // tcgen05 kernel of rows_core.cuh took 93); 48 rows over 128 NVFP4 experts 84
 // us, 2.8 TB/s.  Two blocks an SM are all that the registers hold, and their
 // 16 warps' instruction latency is the bound (issue 40 %).
@@ -29,9 +29,14 @@
 //
 // Decoding: an f16 below 2^-14 is an integer of up to 10 bits times 2^-24, so a
 // field of a record word, masked in place, is the code times 2^(b - 24) with b
-// its lowest bit, and the tokens beside it were scaled by 2^-b: int4 costs 5
-// instructions per 8 codes (4 lop3, 1 shift), int3 3 per 2 codes (the high
-// plane's bit is shifted beside the low plane's).  The zero-point (int3: 4) is
+// its lowest bit; one exact product by 2^14 per two codes makes it a normal
+// number, and the tokens beside it were scaled by 2^-b: int4 costs 9
+// instructions per 8 codes (4 lop3, 1 shift, 4 products), int3 4 per 2 codes
+// (the high plane's bit is shifted beside the low plane's).  Without the product
+// one token is 3 % faster, but the tensor cores line products up by their
+// operands' nominal exponents, and a subnormal's is 2^-14 whatever it holds: the
+// other 15 columns of an MMA lost up to 10 bits beside a token 2^12 times as
+// large (2.4e-5 of sum s (q + z) |x|, 1.7 times the bound).  The zero-point (int3: 4) is
 // taken from the group's sum, sum n x - z sum x, with the tokens' sums of
 // each group from k_few_prep.  NVFP4: the hardware's E2M1 conversion, then
 // dec(e) dec(c) by one f16x2 product (exact: 6 significant bits).
@@ -163,9 +168,10 @@ __device__ __forceinline__ void few_load(FewRaw<FMT>& r, const RowsArgs& a, int 
 }
 
 // Pairs 4 h .. 4 h + 3 of the lane's 16 (rows.cuh) as f16x2; integer formats:
-// the codes n times 2^(b - 24), b as few_field() has it.
+// the codes n times 2^(b - 10), b as few_field() has it.
 template <int FMT>
 __device__ __forceinline__ void few_decode(const FewRaw<FMT>& r, int h, uint32_t (&p)[4]) {
+    constexpr uint32_t UP = 0x74007400u;   // 2^14, twice: normal numbers (see the head of this file)
     if constexpr (FMT == TQ_NVFP4_G16) {   // word h: half a block
         // (a block scale's sign bit is no part of it)
         const uint32_t s = __byte_perm(e4m3x2_f16(r.z & 0x7f7fu), 0u, h < 2 ? 0x1010 : 0x3232);
@@ -180,14 +186,14 @@ __device__ __forceinline__ void few_decode(const FewRaw<FMT>& r, int h, uint32_t
             const int n = 4 * (h & 1) + i, b = few_field(FMT, n);
             const uint32_t lo = (n < 5 ? L : L >> 10) & (0x00030003u << b);
             const uint32_t hi = b + 2 >= n ? H2 << (b + 2 - n) : H2 >> (n - b - 2);
-            p[i] = lo | (hi & (0x00040004u << b));
+            p[i] = f16x2_mul(lo | (hi & (0x00040004u << b)), UP);
         }
     } else {   // word h: codes m and m + 4 of its 8, m = 0 .. 3
         const uint32_t w = r.w[h], w8 = w >> 8;
-        p[0] = w & 0x000f000fu;
-        p[1] = w & 0x00f000f0u;
-        p[2] = w8 & 0x000f000fu;
-        p[3] = w8 & 0x00f000f0u;
+        p[0] = f16x2_mul(w & 0x000f000fu, UP);
+        p[1] = f16x2_mul(w & 0x00f000f0u, UP);
+        p[2] = f16x2_mul(w8 & 0x000f000fu, UP);
+        p[3] = f16x2_mul(w8 & 0x00f000f0u, UP);
     }
 }
 
@@ -204,9 +210,9 @@ k_rows_few(const __grid_constant__ RowsArgs a) {
     using F = FewFmt<FMT>;
     constexpr int PD = 2;
     constexpr bool INT = FMT != TQ_NVFP4_G16;
-    // the fields' 2^-24, half of it to the sums and half to the tokens' power of
+    // the fields' 2^-10, half of it to the sums and half to the tokens' power of
     // two, which goes up to 2^112
-    constexpr float HALF_UNIT = INT ? 4096.f : 1.f;
+    constexpr float HALF_UNIT = INT ? 32.f : 1.f;
     constexpr int VALS = 2 * NB * 4 * 32;   // sums of a warp: 2 tiles of 16 rows x 8 NB tokens
     extern __shared__ float few_smem[];
     float* red = few_smem;                                             // [2][FEW_WARPS][VALS]

@@ -230,3 +230,35 @@ def test_gradient_of_small_probabilities(fmt, R):
     got = tq.tq_head_loss_backward(torch.ones(R, device="cuda"), x, w.handle(tq), labels, lse).double()
     off = (got - want).norm(dim=1)
     assert (off <= err * (1 + BF16) + 2.0 ** -9 * want.norm(dim=1)).all(), (off / want.norm(dim=1)).max()
+
+
+@pytest.mark.parametrize("R", FEW_OR_NOT)
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 18, 2.0 ** 24])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_token_far_above_its_row(fmt, size, R):
+    """One column far above the others, whose weights are zero: what the f16
+    copy keeps of the others, by the header's bounds (few rows: 2^-30 of the
+    largest times s (q + z), since zero-points come from the groups' sums)."""
+    O, I = 90, 264
+    w = ref.Weights(fmt, 1, O, I, 26, "cuda")
+    rec = w.packed.view(O, w.G, -1)
+    if fmt == "int3":   # code 4: v = 0
+        rec[:, 0, 0] &= 0xfc
+        rec[:, 0, 16] |= 1
+    else:               # the low nibble: the zero-point, or E2M1's zero
+        rec[:, 0, 0] = (rec[:, 0, 0] & 0xf0) | (0 if w.zeros is None else w.zeros[0, :, 0])
+    W = w.dense()[0]
+    assert (W[:, 0] == 0).all()
+    x = normal(R, I, 27)
+    x[:, 0] = size
+    top = 2.0 ** -30 * x.double().abs().amax(1, keepdim=True)
+    if R <= 32:
+        z, err = ref.product_few(x, w)
+        err = err + top * (w.spread()[0].sum(1) - W.abs().sum(1))
+    else:
+        z, err = ref.product(x, W, w.G)
+    ref.check(tq.tq_dequant_matmul(x, w.handle(tq), out_dtype=torch.float32), z, err, FP32)
+    if size <= 2.0 ** 12:   # (what tokens may be in earnest: nothing is lost)
+        got = tq.tq_dequant_matmul(x, w.handle(tq), out_dtype=torch.float32).double()
+        exact = (I / 16 + 2 * w.G + 32) * ref.U * (x[:, 1:].double().abs() @ w.spread()[0][:, 1:].T + size * w.spread()[0][:, 0])
+        assert ((got - z).abs() <= exact).all()
