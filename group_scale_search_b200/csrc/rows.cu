@@ -560,18 +560,18 @@ static tq_status check_tokens(const tq_mat* X, int64_t rows, int64_t cols, const
 // a matrix (routed: on average).  Microseconds, few / tensor-memory (the same
 // records again and again, in L2 where they fit):
 //  fewer tiles than SMs: up to 32 rows.  32 rows x 8192 x 4096, int3 32 / 43,
-//    int4 g32 35 / 44, NVFP4 24 / 33; 53 rows over 2 int3 experts 24 / 42.
+//    int4 g32 36 / 44, NVFP4 24 / 33; 53 rows over 2 int3 experts 24 / 43.
 //  one matrix, more tiles: up to 16, int4 g128 up to 32.  Gated 17408 x 5120,
-//    16 rows, int3 71 / 85, g128 46 / 77, g64 58 / 85, g32 79 / 101, NVFP4 46 /
-//    68; 24 rows 88 / 86, 65 / 79, 82 / 87, 116 / 101, 66 / 69.
+//    16 rows, int3 73 / 84, g128 46 / 80, g64 60 / 87, g32 82 / 99, NVFP4 46 /
+//    69; 24 rows 92 / 86, 70 / 79, 84 / 87, 120 / 100, 66 / 69.
 //  experts: their ragged ends fill fewer blocks of 8, which the tensor-memory
-//    kernel pads for nothing.  64 x 2688 x 1856, 8 rows each, int3 99 / 129,
-//    g128 70 / 141, g64 113 / 149, NVFP4 77 / 115; 12 rows int3 134 / 130, g64
-//    167 / 149; 16 rows g128 97 / 145, NVFP4 100 / 118; 24 rows g128 157 / 145,
-//    NVFP4 152 / 117.  g32 spills at 8 tokens (few_blocks_per_sm), hence its
-//    limits: 64 x 2688 x 2048, 4 rows 152 / 173, 8 rows 157 / 172 (not taken);
-//    where rows do not end with a slice, 2688 x 1856, 2 rows 169 / 160, 8 rows
-//    196 / 160.
+//    kernel pads for nothing.  64 x 2688 x 1856, 8 rows each, int3 102 / 130,
+//    g128 73 / 143, g64 115 / 149, NVFP4 77 / 116; 12 rows int3 139 / 130, g64
+//    171 / 150; 16 rows g128 101 / 146, NVFP4 99 / 118; 24 rows g128 162 / 146,
+//    NVFP4 153 / 118.  g32 spills at 8 tokens (few_blocks_per_sm), hence its
+//    limits: 64 x 2688 x 2048, 4 rows 153 / 175, 8 rows 158 / 176 (not taken);
+//    where rows do not end with a slice, 2688 x 1856, 2 rows 171 / 162, 8 rows
+//    199 / 163.
 static int few_blocks(int32_t fmt, const RowsArgs& a) {
     const int64_t per = (a.R + a.E - 1) / a.E, tiles = a.E * tiles_of(a.O, a.projections == 2 ? 64 : 128);
     int64_t most = 32;

@@ -114,7 +114,7 @@ tq_status launch_few_nvfp4(const RowsArgs& a, int nb, int mb, int grid, cudaStre
 // group sums (NVFP4, 16 bytes), unless the grid fills no more than one (17408 x
 // 5120 int4 g128, 14 rows: 45 us against 53; 4096 x 4096, 16 rows: 13 us with
 // one, 17 with two); the other formats take one (11008 x 4096 int4 g64, 12 rows:
-// 29 us against 42).  32: one (16 to 28 bytes of int3, g64 and g32).
+// 29 us against 42).  32: one (24 bytes of g32, 36 of g64).
 __host__ __device__ constexpr bool few_two_fit(int fmt) { return fmt == TQ_INT4_G128_ASYM || fmt == TQ_NVFP4_G16; }
 inline int few_blocks_per_sm(int fmt, int nb, int64_t items, int64_t sms) {
     return nb == 1 ? 2 : nb == 2 && few_two_fit(fmt) && items > sms ? 2 : 1;

@@ -31,12 +31,12 @@
 // clocks.)
 //
 // Measured in sustained passes, the dense ones at the power cap (1.6 to 1.8 GHz;
-// in brackets short runs): gated 2048 rows x 17408 x 5120 int4 g128 690 us, 1.06
+// in brackets short runs): gated 2048 rows x 17408 x 5120 int4 g128 680 us, 1.07
 // PFLOP/s (581), where shared memory is the busiest (78 %, the tensor pipe 65
-// %); a gradient of 8192 rows x 4096 x 4096 int4 g32 304 us, 0.90 PFLOP/s (246;
+// %); a gradient of 8192 rows x 4096 x 4096 int4 g32 296 us, 0.93 PFLOP/s (246;
 // decoding two scales and zero-points a row and step); the loss of 1024 tokens x
 // 65536 x 4096 700 us, 0.79 PFLOP/s (680; exact kind: adding groups); 3001 rows
-// over 128 NVFP4 experts of 2688 x 1856 224 us, 1.7 TB/s of records: what is
+// over 128 NVFP4 experts of 2688 x 1856 222 us, 1.7 TB/s of records: what is
 // bound there is the decoding, with few rows to a weight.
 //
 // Operands are f16: 11 significant bits at the rate of bf16's 8, and powers of
