@@ -416,7 +416,10 @@ tq_status tq_dequant_matmul_backward(const tq_records* W, const tq_mat* dY, cons
  *
  * tq_gated_ffn_backward: from dh (bf16) and x, with g and u recomputed,
  * dx = Wgate^T (dh u act'(g)) + Wup^T (dh act(g)), bf16; the inner gradients
- * are held as 11-bit f16 beside a power of two per token. */
+ * are held as 11-bit f16 beside a power of two per token, that of B =
+ * 1.13 max|dh[t]| |x[t]|_2 sqrt(I) M (M the larger of the two projections';
+ * NVFP4: 6 max block scale |g_gate g_up|): one below 2^-28 B loses bits, by at
+ * most 2^-38 B. */
 enum { TQ_ACT_SILU = 0, TQ_ACT_GELU_TANH = 1 };
 
 size_t tq_gated_ffn_workspace_bytes(const tq_records* gate, int64_t rows);
